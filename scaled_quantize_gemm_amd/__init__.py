@@ -431,3 +431,8 @@ class DelayedScalingState:
 
     def update(self) -> None:
         fp8_recipe_update(self.amax_history, self.scale, self.scale_inv, self.fmts, self.margin)
+
+
+# the MLP block's operators (include/scaled_fp8_mlp.h), marshalled with the helpers above
+from .mlp import (EXPORTED_MLP, fp8_act_backward, fp8_act_backward_workspace, fp8_act_cast_transpose,  # noqa: E402
+                  fp8_gemm_residual, fp8_layernorm, fp8_layernorm_backward, fp8_layernorm_backward_workspace)

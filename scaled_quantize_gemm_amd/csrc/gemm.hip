@@ -20,6 +20,6 @@ extern "C" int fp8_gemm(const uint8_t* A, int fmt_a, const void* a_scale_inv, in
   hipStream_t st = (hipStream_t)stream;
   const int m = (int)M, n = (int)N, k = (int)K;
   if (c_dtype == OUT_F32)
-    return dispatch_mode<EPI_F32, false>(mode, fmt_a, fmt_b, A, B, a_scale_inv, b_scale_inv, ep, m, n, k, st, "fp8_gemm");
-  return dispatch_mode<EPI_BF16, false>(mode, fmt_a, fmt_b, A, B, a_scale_inv, b_scale_inv, ep, m, n, k, st, "fp8_gemm");
+    return dispatch_mode<EPI_F32, EPI_PLAIN>(mode, fmt_a, fmt_b, A, B, a_scale_inv, b_scale_inv, ep, m, n, k, st, "fp8_gemm");
+  return dispatch_mode<EPI_BF16, EPI_PLAIN>(mode, fmt_a, fmt_b, A, B, a_scale_inv, b_scale_inv, ep, m, n, k, st, "fp8_gemm");
 }

@@ -69,7 +69,7 @@ __device__ __forceinline__ bool tile_part_of(int b, int tiles_m, int tiles_n, in
   return true;
 }
 
-template <int MODE, int FA, int FB, int OUT, bool FUSED, int BN, int BM>
+template <int MODE, int FA, int FB, int OUT, int EPI, int BN, int BM>
 __global__ void __launch_bounds__(512, 1) gemm_blk_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                                           const float* __restrict__ sa_p,
                                                           const float* __restrict__ sb_p, const EpiParams ep, int M,
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(512, 1) gemm_blk_kernel(const uint8_t* __restr
   }
 
   // ---- epilogue: acc[i][j][jj] is tile row slab + TI (4g + jj) + i, column slab + NT r + j
-  Epilogue<OUT, FUSED> epi(ep);
+  Epilogue<OUT, EPI> epi(ep);
   float scale = 1.0f;
   if constexpr (TENSOR) scale = sa_p[0] * sb_p[0];
   const int gn = n0 + slab_b + NT * r;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(512, 1) gemm_blk_kernel(const uint8_t* __restr
 // (workload 3's wgrad, 7168 x 7168 x 4096 with 4 tiles per XCD left: 256 -> 243 us).  With
 // half the CUs left busy the halves gained nothing (its forward, 16 tiles per XCD left:
 // 215 -> 220 us), so that case keeps the 256 x 128 tiles.
-template <int MODE, int FA, int FB, int OUT, bool FUSED, int BN, int BM = BLK_BM>
+template <int MODE, int FA, int FB, int OUT, int EPI, int BN, int BM = BLK_BM>
 static int launch_blk(const uint8_t* A, const uint8_t* B, const void* sa, const void* sb, const EpiParams& ep, int M,
                       int N, int K, hipStream_t st, const char* what) {
   const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
@@ -376,16 +376,16 @@ static int launch_blk(const uint8_t* A, const uint8_t* B, const void* sa, const 
     const int whole = per / kXcdCus * kXcdCus;                // tile indices every XCD runs in whole rounds
     const int left = per - whole + ((T & 7) != 0 ? 1 : 0);  // at most this many tiles per XCD after them
     if (whole > 0 && left > 0 && 4 * left <= kXcdCus) {
-      hipLaunchKernelGGL((gemm_blk_kernel<MODE, FA, FB, OUT, FUSED, BN, BM>), dim3(8 * whole), dim3(512), 0, st, A, B,
+      hipLaunchKernelGGL((gemm_blk_kernel<MODE, FA, FB, OUT, EPI, BN, BM>), dim3(8 * whole), dim3(512), 0, st, A, B,
                          fa, fb, ep, M, N, K, tiles_m, tiles_n, 0, 1);
       const int rc = check_launch(what);
       if (rc != FP8_OK) return rc;
-      hipLaunchKernelGGL((gemm_blk_kernel<MODE, FA, FB, OUT, FUSED, 64, BM>), dim3(8 * 2 * left), dim3(512), 0, st, A,
+      hipLaunchKernelGGL((gemm_blk_kernel<MODE, FA, FB, OUT, EPI, 64, BM>), dim3(8 * 2 * left), dim3(512), 0, st, A,
                          B, fa, fb, ep, M, N, K, tiles_m, tiles_n, whole, 2);
       return check_launch(what);
     }
   }
-  hipLaunchKernelGGL((gemm_blk_kernel<MODE, FA, FB, OUT, FUSED, BN, BM>), dim3(tiles_m * tiles_n), dim3(512), 0, st, A, B,
+  hipLaunchKernelGGL((gemm_blk_kernel<MODE, FA, FB, OUT, EPI, BN, BM>), dim3(tiles_m * tiles_n), dim3(512), 0, st, A, B,
                      fa, fb, ep, M, N, K, tiles_m, tiles_n, 0, 1);
   return check_launch(what);
 }

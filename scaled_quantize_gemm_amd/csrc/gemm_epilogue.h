@@ -18,6 +18,8 @@
 //      max-reduced into an amax slot for the delayed recipe ("Transformer Scaling" lesson,
 //      Part 01: each tensor's amax is recorded every step).
 //
+// Residual (fp8_gemm_residual): the fused epilogue without the copy, and y + residual before the store.
+//
 // The kernels run their store loop inside with_act(), which calls it with the activation as a
 // compile-time constant (a runtime test inside the unrolled loop let the compiler evaluate
 // the GELU of every element whatever the activation, and select), and call, per lane, for
@@ -35,6 +37,9 @@ namespace sfp8 {
 // output element types of the GEMM kernels (the public OUT_* values)
 enum { EPI_F32 = OUT_F32, EPI_BF16 = OUT_BF16, EPI_E4M3 = OUT_E4M3, EPI_E5M2 = OUT_E5M2 };
 
+// kinds of epilogue (the kernels' EPI parameter): plain, fused, and fused without aux but with a residual
+enum { EPI_PLAIN = 0, EPI_FUSED = 1, EPI_RESIDUAL = 2 };
+
 struct EpiParams {
   void* C;               // [M][ldc] output, ldc = N (N / 2 for SwiGLU)
   const void* bias;      // fused: [N] fp32 or bf16, or null
@@ -43,6 +48,7 @@ struct EpiParams {
   float* c_amax;         // FP8 output: amax slot (max-reduced into)
   int bias_bf16;         // bias element type is bf16
   int act;               // FP8_ACT_*
+  const void* residual;  // residual: of C's type and shape (may be C)
 };
 
 // GELU, exact form x Phi(x), with erfc from Abramowitz & Stegun 7.1.26 (Hastings' rational
@@ -68,8 +74,9 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-g * 1.44269504088896341f)) * u;
 }
 
-template <int OUT, bool FUSED>
+template <int OUT, int EPI>
 struct Epilogue {
+  static constexpr bool FUSED = EPI != EPI_PLAIN;
   static constexpr bool kFp8 = OUT == EPI_E4M3 || OUT == EPI_E5M2;
   static constexpr int kFmt = OUT == EPI_E5M2 ? FP8_E5M2 : FP8_E4M3;
   const EpiParams p;
@@ -123,7 +130,7 @@ struct Epilogue {
   // bf16 copy of the pre-activation values, row pitch N
   template <int W>
   __device__ __forceinline__ void aux(const float (&v)[W], int gm, int gn, int N, bool full) const {
-    if constexpr (FUSED) {
+    if constexpr (EPI == EPI_FUSED) {
       if (p.aux == nullptr) return;
       store_run<EPI_BF16, W>(p.aux, (size_t)gm * N + gn, v, full, N - gn);
     }
@@ -137,6 +144,7 @@ struct Epilogue {
       float o[W / 2];
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) o[i] = swiglu(v[2 * i], v[2 * i + 1]);
+      add_residual<W / 2>(o, (size_t)gm * (N / 2) + gn / 2, full, (N - gn) / 2);
       // output column gn/2 + i exists iff its up column gn + 2i + 1 does
       emit<W / 2>(o, (size_t)gm * (N / 2) + gn / 2, full, (N - gn) / 2);
     } else {
@@ -144,6 +152,7 @@ struct Epilogue {
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = gelu_exact(v[i]);
       }
+      add_residual<W>(v, (size_t)gm * N + gn, full, N - gn);
       emit<W>(v, (size_t)gm * N + gn, full, N - gn);
     }
   }
@@ -170,6 +179,19 @@ struct Epilogue {
   }
 
  private:
+  // + the residual at element offset `at` (C's own layout and type); each element is read by the lane that
+  // then writes it, so C may be the residual
+  template <int W>
+  __device__ __forceinline__ void add_residual(float (&v)[W], size_t at, bool full, int avail) const {
+    if constexpr (EPI == EPI_RESIDUAL) {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (full || i < avail)
+          v[i] += OUT == EPI_BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.residual)[at + i] << 16)
+                                  : static_cast<const float*>(p.residual)[at + i];
+    }
+  }
+
   // W values to element offset `at` of the output; `avail` = how many of them exist
   template <int W>
   __device__ __forceinline__ void emit(const float (&v)[W], size_t at, bool full, int avail) {

@@ -29,7 +29,7 @@ constexpr int64_t kSmallTileMax = 256;
 // of at least 256 of its tiles and for MX; the 256 x 128 / 256 x 64 kernel (gemm_blk.h) for the
 // blockwise modes and smaller per-tensor problems; the 128 x 128 kernel (gemm_small.h) where
 // neither applies
-template <int MODE, int FA, int FB, int OUT, bool FUSED>
+template <int MODE, int FA, int FB, int OUT, int EPI>
 static int launch_gemm(const uint8_t* A, const uint8_t* B, const void* sa, const void* sb, const EpiParams& ep, int M,
                        int N, int K, hipStream_t st, const char* what) {
   if constexpr (MODE == MODE_TENSOR) {
@@ -44,10 +44,10 @@ static int launch_gemm(const uint8_t* A, const uint8_t* B, const void* sa, const
       if (tiles < kNarrowTiles) {
         const int64_t small = (int64_t)((M + 127) / 128) * ((N + 63) / 64);
         if (small <= kSmallTileMax)
-          return launch_blk<MODE, FA, FB, OUT, FUSED, 64, 128>(A, B, sa, sb, ep, M, N, K, st, what);
-        return launch_blk<MODE, FA, FB, OUT, FUSED, 64>(A, B, sa, sb, ep, M, N, K, st, what);
+          return launch_blk<MODE, FA, FB, OUT, EPI, 64, 128>(A, B, sa, sb, ep, M, N, K, st, what);
+        return launch_blk<MODE, FA, FB, OUT, EPI, 64>(A, B, sa, sb, ep, M, N, K, st, what);
       }
-      return launch_blk<MODE, FA, FB, OUT, FUSED, BLK_BN>(A, B, sa, sb, ep, M, N, K, st, what);
+      return launch_blk<MODE, FA, FB, OUT, EPI, BLK_BN>(A, B, sa, sb, ep, M, N, K, st, what);
     }
   }
   if constexpr (MODE == MODE_TENSOR || MODE == MODE_MX) {
@@ -59,7 +59,7 @@ static int launch_gemm(const uint8_t* A, const uint8_t* B, const void* sa, const
       // offsets; beyond that the 128 x 128 kernel (64-bit addressing) takes the problem
       const int64_t mn = M > N ? M : N;
       const bool offsets32 = 256ll * K < (1ll << 32) && (MODE != MODE_MX || (int64_t)(K / 32) * mn < (1ll << 32));
-      if (offsets32) return launch_w4<MODE, FA, FB, OUT, FUSED>(A, B, sa, sb, ep, M, N, K, st, what);
+      if (offsets32) return launch_w4<MODE, FA, FB, OUT, EPI>(A, B, sa, sb, ep, M, N, K, st, what);
     }
   }
   if constexpr (MODE == MODE_BLOCK || MODE == MODE_TILE2) {
@@ -67,13 +67,13 @@ static int launch_gemm(const uint8_t* A, const uint8_t* B, const void* sa, const
     // a tile's rows and a stage's scales
     const int64_t mn = M > N ? M : N;
     const bool offsets32 = 256ll * K < (1ll << 32) && (int64_t)(K / 128) * mn * 4 < (1ll << 32);
-    if (offsets32) return launch_blk<MODE, FA, FB, OUT, FUSED, BLK_BN>(A, B, sa, sb, ep, M, N, K, st, what);
+    if (offsets32) return launch_blk<MODE, FA, FB, OUT, EPI, BLK_BN>(A, B, sa, sb, ep, M, N, K, st, what);
   }
   constexpr int BM = 128, BN = 128;
   using Cfg = GemmCfg<BM, BN>;
   dim3 grid((N + BN - 1) / BN, (M + BM - 1) / BM);
   const size_t lds = 2 * (Cfg::LDS_A + Cfg::LDS_B);
-  hipLaunchKernelGGL((gemm_kernel<BM, BN, MODE, FA, FB, OUT, FUSED>), grid, dim3(256), lds, st, A, B, sa, sb, ep, M, N, K);
+  hipLaunchKernelGGL((gemm_kernel<BM, BN, MODE, FA, FB, OUT, EPI>), grid, dim3(256), lds, st, A, B, sa, sb, ep, M, N, K);
   return check_launch(what);
 }
 
@@ -115,25 +115,25 @@ static inline int gemm_check(const char* what, const uint8_t* A, int fmt_a, cons
   return FP8_OK;
 }
 
-template <int MODE, int OUT, bool FUSED>
+template <int MODE, int OUT, int EPI>
 static int dispatch_fmt(int fa, int fb, const uint8_t* A, const uint8_t* B, const void* sa, const void* sb,
                         const EpiParams& ep, int M, int N, int K, hipStream_t st, const char* what) {
-  if (fa == FP8_E4M3 && fb == FP8_E4M3) return launch_gemm<MODE, 0, 0, OUT, FUSED>(A, B, sa, sb, ep, M, N, K, st, what);
-  if (fa == FP8_E5M2 && fb == FP8_E4M3) return launch_gemm<MODE, 1, 0, OUT, FUSED>(A, B, sa, sb, ep, M, N, K, st, what);
-  if constexpr (!FUSED) {  // the fused entry point takes B in E4M3 only (checked on the host)
-    if (fa == FP8_E4M3 && fb == FP8_E5M2) return launch_gemm<MODE, 0, 1, OUT, FUSED>(A, B, sa, sb, ep, M, N, K, st, what);
-    return launch_gemm<MODE, 1, 1, OUT, FUSED>(A, B, sa, sb, ep, M, N, K, st, what);
+  if (fa == FP8_E4M3 && fb == FP8_E4M3) return launch_gemm<MODE, 0, 0, OUT, EPI>(A, B, sa, sb, ep, M, N, K, st, what);
+  if (fa == FP8_E5M2 && fb == FP8_E4M3) return launch_gemm<MODE, 1, 0, OUT, EPI>(A, B, sa, sb, ep, M, N, K, st, what);
+  if constexpr (EPI == EPI_PLAIN) {  // the fused entry points take B in E4M3 only (checked on the host)
+    if (fa == FP8_E4M3 && fb == FP8_E5M2) return launch_gemm<MODE, 0, 1, OUT, EPI>(A, B, sa, sb, ep, M, N, K, st, what);
+    return launch_gemm<MODE, 1, 1, OUT, EPI>(A, B, sa, sb, ep, M, N, K, st, what);
   }
   return set_error(FP8_ERR_ARG, "%s: B must be E4M3", what);
 }
 
-template <int OUT, bool FUSED>
+template <int OUT, int EPI>
 static int dispatch_mode(int mode, int fa, int fb, const uint8_t* A, const uint8_t* B, const void* sa, const void* sb,
                          const EpiParams& ep, int M, int N, int K, hipStream_t st, const char* what) {
-  if (mode == MODE_TENSOR) return dispatch_fmt<MODE_TENSOR, OUT, FUSED>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
-  if (mode == MODE_BLOCK) return dispatch_fmt<MODE_BLOCK, OUT, FUSED>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
-  if (mode == MODE_TILE2) return dispatch_fmt<MODE_TILE2, OUT, FUSED>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
-  return dispatch_fmt<MODE_MX, OUT, FUSED>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
+  if (mode == MODE_TENSOR) return dispatch_fmt<MODE_TENSOR, OUT, EPI>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
+  if (mode == MODE_BLOCK) return dispatch_fmt<MODE_BLOCK, OUT, EPI>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
+  if (mode == MODE_TILE2) return dispatch_fmt<MODE_TILE2, OUT, EPI>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
+  return dispatch_fmt<MODE_MX, OUT, EPI>(fa, fb, A, B, sa, sb, ep, M, N, K, st, what);
 }
 
 }  // namespace sfp8

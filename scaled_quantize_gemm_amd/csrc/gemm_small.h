@@ -45,7 +45,7 @@ struct GemmCfg {
 // over 16 consecutive rows for each row parity (64 banks), so fragment reads do not conflict
 __device__ __forceinline__ int swz(int row, int c) { return row * 128 + ((c ^ (((row >> 1) ^ ((row & 1) << 2)) & 7)) << 4); }
 
-template <int BM, int BN, int MODE, int FA, int FB, int OUT, bool FUSED>
+template <int BM, int BN, int MODE, int FA, int FB, int OUT, int EPI>
 __global__ void __launch_bounds__(256) gemm_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                                    const void* __restrict__ sa_p, const void* __restrict__ sb_p,
                                                    const EpiParams ep, int M, int N, int K) {
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) gemm_kernel(const uint8_t* __restrict__ A
   }
 
   // ---- epilogue: lane (g, r) holds column 16j + r of rows 4g + jj of tile (i, j)
-  Epilogue<OUT, FUSED> epi(ep);
+  Epilogue<OUT, EPI> epi(ep);
   float s = 1.0f;
   if constexpr (MODE == MODE_TENSOR) s = *static_cast<const float*>(sa_p) * *static_cast<const float*>(sb_p);
   epi.with_act([&](auto act_c) {

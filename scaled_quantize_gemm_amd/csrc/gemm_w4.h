@@ -56,7 +56,7 @@ constexpr int kW4Last = 13;
 
 __device__ __forceinline__ int w4_swz(int row) { return ((row >> 1) ^ ((row & 1) << 2)) & 7; }
 
-template <int MODE, int FA, int FB, int OUT, bool FUSED>
+template <int MODE, int FA, int FB, int OUT, int EPI>
 __global__ void __launch_bounds__(256, 1) gemm_w4_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                                          const void* __restrict__ sa_p, const void* __restrict__ sb_p,
                                                          const EpiParams ep, int M, int N, int K, int tiles_m,
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(256, 1) gemm_w4_kernel(const uint8_t* __restri
   //      column 128 wn + 4r + j: each lane writes runs of 4 columns.  The stores are
   //      nontemporal: C goes on to HBM while other tiles still compute, instead of staying
   //      dirty in the caches for whatever kernel runs next to write back.
-  Epilogue<OUT, FUSED> epi(ep);
+  Epilogue<OUT, EPI> epi(ep);
   float scale = 1.0f;
   if constexpr (MODE == MODE_TENSOR) scale = *static_cast<const float*>(sa_p) * *static_cast<const float*>(sb_p);
   const int gn = n0 + wn * 128 + 4 * r;
@@ -338,11 +338,11 @@ __global__ void __launch_bounds__(256, 1) gemm_w4_kernel(const uint8_t* __restri
 
 // launch over the tiles of C (per-tensor or MX); the caller has checked that the kernel
 // applies (M, N >= 4; MX: multiples of 4; 32-bit row and scale offsets)
-template <int MODE, int FA, int FB, int OUT, bool FUSED>
+template <int MODE, int FA, int FB, int OUT, int EPI>
 static int launch_w4(const uint8_t* A, const uint8_t* B, const void* sa, const void* sb, const EpiParams& ep, int M,
                      int N, int K, hipStream_t st, const char* what) {
   const int tiles_m = (M + W4_BM - 1) / W4_BM, tiles_n = (N + W4_BN - 1) / W4_BN;
-  hipLaunchKernelGGL((gemm_w4_kernel<MODE, FA, FB, OUT, FUSED>), dim3(tiles_m * tiles_n), dim3(256), 0, st, A, B, sa,
+  hipLaunchKernelGGL((gemm_w4_kernel<MODE, FA, FB, OUT, EPI>), dim3(tiles_m * tiles_n), dim3(256), 0, st, A, B, sa,
                      sb, ep, M, N, K, tiles_m, tiles_n);
   return check_launch(what);
 }
