@@ -239,6 +239,6 @@ extern "C" int fp8_act_backward(const void* dh, const void* pre, int dtype, int6
     if (rc2 != FP8_OK) return rc2;
   }
   if (dbias == nullptr) return FP8_OK;
-  launch_col_reduce(part, (int)((rows + kActTile - 1) / kActTile), cols, dbias, cols, nullptr, st);
+  launch_col_reduce(part, (int)((rows + kActTile - 1) / kActTile), 1, cols, cols, dbias, nullptr, st);
   return check_launch(what);
 }
