@@ -7,107 +7,341 @@
 // and the result goes to FP8 under the cast rules of quantize.hip, per tensor (delayed scale, amax into a
 // slot) or in 1x128 runs (its own for q and for the transposed copy).
 //
-// One block per 128 x 128 tile of the result, which it computes into LDS in fp32 and reads by rows for q and
-// by columns for qT.
+// Bound by memory: pre and dh once in, two copies of the codes out.  One 512-thread block per 128 x 128 tile of the
+// result: thread t computes rows t/16 + 32p (p = 0..3), columns 8(t%16)..+8, from 16-byte loads, casts them, writes q,
+// and puts the codes for qT into an LDS tile (dword pitch 33) that leaves with 4x4 byte transposes, 128 contiguous bytes of a
+// qT row per 32 lanes.  Per tensor the scale is known beforehand, so a value is cast as soon as it is computed
+// and a block's next tile is loaded before it transposes the current one; in 1x128 runs the thread's 32 values wait in
+// registers for the row and column maxima.  The bias gradient's column sums go through lane exchanges and LDS
+// to one partial row per tile row, joined by a second kernel in order.
+//
+// Any size and alignment: vectors are loaded and stored at the element's alignment (the hardware takes them at any
+// address), tiles at the edge test their rows and chunks, and a row's last partial chunk goes by element.
+#include <algorithm>
+
 #include "act_math.h"
 #include "col_reduce.h"
+#include "quant_rules.h"
 
 namespace sfp8 {
 
-constexpr int kActTile = 128, kActPitch = 129;
+constexpr int kActTile = 128, kActPitch = 33;
 // what a kernel computes from its inputs
 enum { ACT_FWD_GELU = 0, ACT_FWD_SWIGLU = 1, ACT_BWD_NONE = 2, ACT_BWD_GELU = 3, ACT_BWD_SWIGLU = 4 };
 
-template <bool BF16>
-__device__ __forceinline__ float act_ld(const void* __restrict__ p, int64_t i) {
-  if constexpr (BF16) return __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
-  else return static_cast<const float*>(p)[i];
-}
+// N consecutive elements as loaded (N = 4, 8, 16), kept packed until the arithmetic
+template <bool BF16, int N>
+struct ActRaw {
+  static constexpr int kWords = BF16 ? N / 2 : N;
+  uint32_t w[kWords];
+};
 
-// element (r, c) of the result [rows][cols]
-template <int OP, bool BF16>
-__device__ __forceinline__ float act_at(const void* __restrict__ dh, const void* __restrict__ pre, int64_t r, int64_t c,
-                                        int64_t cols) {
-  if constexpr (OP == ACT_FWD_GELU) return act_gelu(act_ld<BF16>(pre, r * cols + c));
-  if constexpr (OP == ACT_FWD_SWIGLU)
-    return act_swiglu(act_ld<BF16>(pre, 2 * (r * cols + c)), act_ld<BF16>(pre, 2 * (r * cols + c) + 1));
-  if constexpr (OP == ACT_BWD_NONE) return act_ld<BF16>(dh, r * cols + c);
-  if constexpr (OP == ACT_BWD_GELU) return act_ld<BF16>(dh, r * cols + c) * act_gelu_grad(act_ld<BF16>(pre, r * cols + c));
-  if constexpr (OP == ACT_BWD_SWIGLU) {
-    const int64_t f = r * (cols >> 1) + (c >> 1);
-    float dg, du;
-    act_swiglu_grad(act_ld<BF16>(dh, f), act_ld<BF16>(pre, 2 * f), act_ld<BF16>(pre, 2 * f + 1), dg, du);
-    return (c & 1) ? du : dg;
+template <int N>
+struct ActVec;
+template <>
+struct ActVec<2> {
+  typedef u32x2 type __attribute__((aligned(2)));
+};
+template <>
+struct ActVec<4> {
+  typedef u32x4 type __attribute__((aligned(2)));
+};
+
+// elements c .. c+N-1 of a row of `cols` at p (those past its end read as 0)
+template <bool BF16, int N, bool EDGE>
+__device__ __forceinline__ void act_load(const void* row, int64_t c, int64_t cols, ActRaw<BF16, N>& r) {
+  constexpr int W = ActRaw<BF16, N>::kWords, V = W < 4 ? W : 4;
+  if (!EDGE || c + N <= cols) {
+    const char* p = static_cast<const char*>(row) + c * (BF16 ? 2 : 4);
+    typedef typename ActVec<V>::type T;
+#pragma unroll
+    for (int i = 0; i < W / V; ++i) {
+      const auto v = __builtin_nontemporal_load(reinterpret_cast<const T*>(p) + i);
+#pragma unroll
+      for (int j = 0; j < V; ++j) r.w[V * i + j] = v[j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) r.w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < cols) {
+        if constexpr (BF16) r.w[i / 2] |= (uint32_t)static_cast<const uint16_t*>(row)[c + i] << (16 * (i & 1));
+        else r.w[i] = static_cast<const uint32_t*>(row)[c + i];
+      }
   }
 }
 
-template <int FMT>
-__device__ __forceinline__ uint8_t act_code(float v, float s) {
-  const uint32_t b = __float_as_uint(v);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return (uint8_t)nan_code(b);
-  return (uint8_t)cvt_pair<FMT, false>(v * s, 0.0f, 0u);
+template <bool BF16, int N>
+__device__ __forceinline__ float act_elem(const ActRaw<BF16, N>& r, int i) {
+  if constexpr (BF16) return (i & 1) ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+  else return __uint_as_float(r.w[i]);
 }
 
-template <int OP, int FMT, bool BF16, bool TILE>
-__global__ void __launch_bounds__(256) act_ct_kernel(const void* __restrict__ dh, const void* __restrict__ pre,
+// the inputs of 8 adjacent results of a row
+template <int OP, bool BF16>
+struct ActIn {
+  static constexpr bool kPre = OP != ACT_BWD_NONE, kDh = OP >= ACT_BWD_NONE;
+  static constexpr int kPreN = OP == ACT_FWD_SWIGLU ? 16 : 8, kDhN = OP == ACT_BWD_SWIGLU ? 4 : 8;
+  ActRaw<BF16, kPreN> pre;
+  ActRaw<BF16, kDhN> dh;
+
+  // results (row, c .. c+7) of [rows][cols]
+  template <bool EDGE>
+  __device__ __forceinline__ void load(const void* dhp, const void* prep, int64_t row, int64_t c, int64_t cols) {
+    constexpr int E = BF16 ? 2 : 4;
+    if constexpr (kPre) {
+      constexpr int64_t f = kPreN / 8;
+      act_load<BF16, kPreN, EDGE>(static_cast<const char*>(prep) + row * cols * f * E, c * f, cols * f, pre);
+    }
+    if constexpr (kDh) {
+      constexpr int64_t f = 8 / kDhN;
+      act_load<BF16, kDhN, EDGE>(static_cast<const char*>(dhp) + row * (cols / f) * E, c / f, cols / f, dh);
+    }
+  }
+  // zero inputs: every result 0
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < ActRaw<BF16, kPreN>::kWords; ++i) pre.w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < ActRaw<BF16, kDhN>::kWords; ++i) dh.w[i] = 0u;
+  }
+  __device__ __forceinline__ void results(float (&v)[8]) const {
+    if constexpr (OP == ACT_FWD_GELU) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_gelu(act_elem(pre, i));
+    } else if constexpr (OP == ACT_FWD_SWIGLU) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_swiglu(act_elem(pre, 2 * i), act_elem(pre, 2 * i + 1));
+    } else if constexpr (OP == ACT_BWD_NONE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_elem(dh, i);
+    } else if constexpr (OP == ACT_BWD_GELU) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_elem(dh, i) * act_gelu_grad(act_elem(pre, i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        act_swiglu_grad(act_elem(dh, i), act_elem(pre, 2 * i), act_elem(pre, 2 * i + 1), v[2 * i], v[2 * i + 1]);
+    }
+  }
+};
+
+// |x| bits of the largest of 8 values (NaN above everything)
+__device__ __forceinline__ uint32_t act_amax8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = m > abs_bits(v[i]) ? m : abs_bits(v[i]);
+  return m;
+}
+
+template <int FMT>
+__device__ __forceinline__ u32x2 act_cast8(const float (&v)[8], const float (&s)[8], uint32_t amax_bits) {
+  uint32_t w0 = cvt4<FMT>(v[0] * s[0], v[1] * s[1], v[2] * s[2], v[3] * s[3]);
+  uint32_t w1 = cvt4<FMT>(v[4] * s[4], v[5] * s[5], v[6] * s[6], v[7] * s[7]);
+  if (amax_bits > 0x7F800000u) {
+    w0 = patch_nan4(w0, &v[0]);
+    w1 = patch_nan4(w1, &v[4]);
+  }
+  return u32x2{w0, w1};
+}
+
+template <int OP, int FMT, bool BF16, bool TILE, bool EDGE>
+__global__ void __launch_bounds__(512) act_ct_kernel(const void* __restrict__ dh, const void* __restrict__ pre,
                                                      int64_t rows, int64_t cols, const float* __restrict__ scale_p,
                                                      uint32_t* __restrict__ amax_slot, uint8_t* __restrict__ q,
                                                      float* __restrict__ q_sinv, uint8_t* __restrict__ qT,
                                                      float* __restrict__ qT_sinv, float* __restrict__ part) {
-  __shared__ float v[kActTile * kActPitch];
-  __shared__ float srow[kActTile], scol[kActTile];
-  __shared__ uint32_t red[4];
-  const int t = threadIdx.x;
-  const int64_t tiles_c = (cols + kActTile - 1) / kActTile;
-  const int64_t rb = blockIdx.x / tiles_c, kb = blockIdx.x % tiles_c;
-  const int64_t r0 = rb * kActTile, c0 = kb * kActTile;
-  uint32_t mx = 0;
-  for (int e = t; e < kActTile * kActTile; e += 256) {
-    const int r = e >> 7, c = e & 127;
-    float x = 0.0f;
-    if (r0 + r < rows && c0 + c < cols) x = act_at<OP, BF16>(dh, pre, r0 + r, c0 + c, cols);
-    v[r * kActPitch + c] = x;
-    mx = mx > abs_bits(x) ? mx : abs_bits(x);
-  }
-  __syncthreads();
-  if constexpr (TILE) {
-    uint32_t a = 0;
-    for (int i = 0; i < kActTile; ++i) {
-      const uint32_t b = abs_bits(t < 128 ? v[t * kActPitch + i] : v[i * kActPitch + t - 128]);
-      a = a > b ? a : b;
-    }
-    float s, si;
-    current_scale<FMT>(a, s, si);
-    if (t < 128) {
-      srow[t] = s;
-      q_sinv[kb * rows + r0 + t] = si;
-    } else {
-      scol[t - 128] = s;
-      qT_sinv[rb * cols + c0 + t - 128] = si;
-    }
-  } else {
-    if (t < 128) srow[t] = scol[t] = *scale_p;
-    mx = wave_max_u32(mx);
-    if ((t & 63) == 0) red[t >> 6] = mx;
-  }
-  __syncthreads();
-  if constexpr (!TILE) {
-    if (t == 0 && amax_slot != nullptr) {
-      uint32_t b = red[0];
+  typedef u32x2 q_t __attribute__((aligned(1)));
+  typedef uint32_t qt_t __attribute__((aligned(1)));
+  static_assert(!(TILE && EDGE), "1x128 runs need whole tiles");
+  __shared__ uint32_t lds[kActTile * kActPitch];
+  __shared__ float csum[8][kActTile];
+  __shared__ uint32_t cred[8][kActTile];
+  __shared__ float cscale[kActTile];
+  const int64_t nkb = (cols + kActTile - 1) / kActTile, nrb = (rows + kActTile - 1) / kActTile, ntiles = nkb * nrb;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int r16 = t >> 4, cg = t & 15;
+  // tiles in bands of 8 tile rows, walked column by column: the blocks in flight write 1 KB runs of a qT row
+  auto tile_rc = [&](int64_t ix, int64_t& rb, int64_t& kb) {
+    constexpr int64_t SR = 8;
+    const int64_t band = ix / (SR * nkb), first = band * SR;
+    const int64_t h = nrb - first < SR ? nrb - first : SR;
+    const int64_t in = ix - band * SR * nkb;
+    rb = first + in % h;
+    kb = in / h;
+  };
+  ActIn<OP, BF16> in[4];
+  auto load_tile = [&](int64_t ix) {
+    int64_t rb, kb;
+    tile_rc(ix, rb, kb);
+    const int64_t c = kb * kActTile + cg * 8;
 #pragma unroll
-      for (int i = 1; i < 4; ++i) b = b > red[i] ? b : red[i];
-      if (b > __hip_atomic_load(amax_slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(amax_slot, b);
+    for (int p = 0; p < 4; ++p) {
+      const int64_t r = rb * kActTile + r16 + 32 * p;
+      if (!EDGE || (r < rows && c < cols)) in[p].template load<EDGE>(dh, pre, r, c, cols);
+      else in[p].zero();
+    }
+  };
+  float s8[8];
+  if constexpr (!TILE) {
+    const float s = *scale_p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s8[e] = s;
+  }
+  uint32_t amax_acc = 0;
+  load_tile(blockIdx.x);
+  for (int64_t ix = blockIdx.x; ix < ntiles; ix += gridDim.x) {
+    if (ix != (int64_t)blockIdx.x) __syncthreads();  // the previous tile's transpose is done with the LDS
+    int64_t rb, kb;
+    tile_rc(ix, rb, kb);
+    const int64_t r0 = rb * kActTile, c0 = kb * kActTile;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    // q codes of row r16 + 32p at the tile's columns 8 cg
+    auto store_q = [&](int p, u32x2 w) {
+      const int64_t r = r0 + r16 + 32 * p, c = c0 + cg * 8;
+      uint8_t* at = q + r * cols + c;
+      if (!EDGE || (r < rows && c + 8 <= cols)) {
+        __builtin_nontemporal_store(w, reinterpret_cast<q_t*>(at));
+      } else if (r < rows) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) at[i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+      }
+    };
+    if constexpr (!TILE) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        float v[8];
+        in[p].results(v);
+        const uint32_t m = act_amax8(v);
+        amax_acc = amax_acc > m ? amax_acc : m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        const u32x2 w = act_cast8<FMT>(v, s8, m);
+        store_q(p, w);
+        lds[(r16 + 32 * p) * kActPitch + cg * 2] = w.x;
+        lds[(r16 + 32 * p) * kActPitch + cg * 2 + 1] = w.y;
+      }
+      if (ix + gridDim.x < ntiles) load_tile(ix + gridDim.x);
+    } else {
+      float v[4][8], srow[4];
+      uint32_t m[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        in[p].results(v[p]);
+        m[p] = act_amax8(v[p]);
+        float si;
+        current_scale<FMT>(group_max_u32<16>(m[p]), srow[p], si);
+        if (cg == 0) q_sinv[kb * rows + r0 + r16 + 32 * p] = si;  // [cols/128][rows]
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[p][e];
+      }
+      if (ix + gridDim.x < ntiles) load_tile(ix + gridDim.x);
+      // column runs: this thread's 4 rows, the wave's 4 lane groups, then the 8 waves
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) c = c > abs_bits(v[p][e]) ? c : abs_bits(v[p][e]);
+        uint32_t o = (uint32_t)__shfl_xor((int)c, 16, 64);
+        c = c > o ? c : o;
+        o = (uint32_t)__shfl_xor((int)c, 32, 64);
+        c = c > o ? c : o;
+        if (lane < 16) cred[wave][cg * 8 + e] = c;
+      }
+      __syncthreads();
+      if (t < kActTile) {
+        uint32_t c = cred[0][t];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) c = c > cred[w][t] ? c : cred[w][t];
+        float sc, si;
+        current_scale<FMT>(c, sc, si);
+        cscale[t] = sc;
+        qT_sinv[rb * cols + c0 + t] = si;  // [rows/128][cols]
+      }
+      __syncthreads();
+      float scol[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) scol[e] = cscale[cg * 8 + e];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        float sr[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sr[e] = srow[p];
+        store_q(p, act_cast8<FMT>(v[p], sr, m[p]));
+        const u32x2 w = act_cast8<FMT>(v[p], scol, m[p]);
+        lds[(r16 + 32 * p) * kActPitch + cg * 2] = w.x;
+        lds[(r16 + 32 * p) * kActPitch + cg * 2 + 1] = w.y;
+      }
+    }
+    if (part != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum[e] += __shfl_xor(sum[e], 16, 64);
+        sum[e] += __shfl_xor(sum[e], 32, 64);
+      }
+      if (lane < 16) {
+        *reinterpret_cast<float4*>(&csum[wave][cg * 8]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        *reinterpret_cast<float4*>(&csum[wave][cg * 8 + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+      }
+    }
+    __syncthreads();
+    if (part != nullptr && t < kActTile && (!EDGE || c0 + t < cols)) {
+      float a = csum[0][t];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) a += csum[w][t];
+      part[rb * cols + c0 + t] = a;
+    }
+    // transpose: 4 source rows x 4 source columns per dword quad
+    const int rg = t & 31, cgt = t >> 5;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int cq = cgt + 16 * h;  // columns 4cq .. 4cq+3 of the tile
+      const uint32_t d0 = lds[(4 * rg + 0) * kActPitch + cq];
+      const uint32_t d1 = lds[(4 * rg + 1) * kActPitch + cq];
+      const uint32_t d2 = lds[(4 * rg + 2) * kActPitch + cq];
+      const uint32_t d3 = lds[(4 * rg + 3) * kActPitch + cq];
+      const uint32_t lo01 = __builtin_amdgcn_perm(d1, d0, 0x05010400u);
+      const uint32_t hi01 = __builtin_amdgcn_perm(d1, d0, 0x07030602u);
+      const uint32_t lo23 = __builtin_amdgcn_perm(d3, d2, 0x05010400u);
+      const uint32_t hi23 = __builtin_amdgcn_perm(d3, d2, 0x07030602u);
+      uint32_t o[4];
+      o[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+      o[1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+      o[2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+      o[3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+      const int64_t r = r0 + 4 * rg;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t c = c0 + 4 * cq + j;
+        uint8_t* at = qT + c * rows + r;
+        if (!EDGE || (c < cols && r + 4 <= rows)) {
+          __builtin_nontemporal_store(o[j], reinterpret_cast<qt_t*>(at));
+        } else if (c < cols) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (r + i < rows) at[i] = (uint8_t)(o[j] >> (8 * i));
+        }
+      }
     }
   }
-  if (part != nullptr && t < 128 && c0 + t < cols) {
-    float s = 0.0f;
-    for (int r = 0; r < kActTile; ++r) s += v[r * kActPitch + t];
-    part[rb * cols + c0 + t] = s;
-  }
-  for (int e = t; e < kActTile * kActTile; e += 256) {
-    const int i = e >> 7, j = e & 127;
-    if (r0 + i < rows && c0 + j < cols) q[(r0 + i) * cols + c0 + j] = act_code<FMT>(v[i * kActPitch + j], srow[i]);
-    if (r0 + j < rows && c0 + i < cols) qT[(c0 + i) * rows + r0 + j] = act_code<FMT>(v[j * kActPitch + i], scol[i]);
+  // per tensor: the block's amax into the slot with one atomic (a plain read first: most blocks do not raise it)
+  if constexpr (!TILE) {
+    if (amax_slot != nullptr) {
+      const uint32_t mx = wave_max_u32(amax_acc);
+      __syncthreads();
+      if (lane == 0) cred[wave][0] = mx;
+      __syncthreads();
+      if (t == 0) {
+        uint32_t bm = cred[0][0];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) bm = bm > cred[w][0] ? bm : cred[w][0];
+        if (bm > __hip_atomic_load(amax_slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(amax_slot, bm);
+      }
+    }
   }
 }
 
@@ -126,15 +360,17 @@ struct ActArgs {
 
 template <int OP, int FMT, bool BF16>
 static void launch_act(const ActArgs& a, bool tile) {
-  const int64_t blocks = ((a.rows + kActTile - 1) / kActTile) * ((a.cols + kActTile - 1) / kActTile);
-  if (tile)
-    hipLaunchKernelGGL((act_ct_kernel<OP, FMT, BF16, true>), dim3((unsigned)blocks), dim3(256), 0, a.st, a.dh, a.pre,
-                       a.rows, a.cols, a.scale, reinterpret_cast<uint32_t*>(a.amax), a.q, a.q_sinv, a.qT, a.qT_sinv,
-                       a.part);
-  else
-    hipLaunchKernelGGL((act_ct_kernel<OP, FMT, BF16, false>), dim3((unsigned)blocks), dim3(256), 0, a.st, a.dh, a.pre,
-                       a.rows, a.cols, a.scale, reinterpret_cast<uint32_t*>(a.amax), a.q, a.q_sinv, a.qT, a.qT_sinv,
-                       a.part);
+  const int64_t tiles = ((a.rows + kActTile - 1) / kActTile) * ((a.cols + kActTile - 1) / kActTile);
+  const int64_t cap = 3ll * device_cus();
+  const dim3 grid((unsigned)std::min(tiles, cap));
+  uint32_t* slot = reinterpret_cast<uint32_t*>(a.amax);
+#define SFP8_ACT(TILE, EDGE)                                                                                          \
+  hipLaunchKernelGGL((act_ct_kernel<OP, FMT, BF16, TILE, EDGE>), grid, dim3(512), 0, a.st, a.dh, a.pre, a.rows, a.cols, \
+                     a.scale, slot, a.q, a.q_sinv, a.qT, a.qT_sinv, a.part)
+  if (tile) SFP8_ACT(true, false);
+  else if (a.rows % kActTile == 0 && a.cols % kActTile == 0) SFP8_ACT(false, false);
+  else SFP8_ACT(false, true);
+#undef SFP8_ACT
 }
 
 template <int OP>
