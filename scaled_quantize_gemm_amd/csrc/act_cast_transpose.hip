@@ -127,23 +127,60 @@ struct ActIn {
   }
 };
 
-// |x| bits of the largest of 8 values (NaN above everything)
+// max of |a|, |b|, |c| that keeps a NaN (one v_maximum3_f32); as bits NaN is above everything
+__device__ __forceinline__ float act_max3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b)),
+                                       __builtin_fabsf(c));
+}
 __device__ __forceinline__ uint32_t act_amax8(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = m > abs_bits(v[i]) ? m : abs_bits(v[i]);
-  return m;
+  const float m = act_max3(act_max3(v[0], v[1], v[2]), v[3], v[4]);
+  return abs_bits(act_max3(act_max3(m, v[5], v[6]), v[7], v[7]));
 }
 
-template <int FMT>
-__device__ __forceinline__ u32x2 act_cast8(const float (&v)[8], const float (&s)[8], uint32_t amax_bits) {
-  uint32_t w0 = cvt4<FMT>(v[0] * s[0], v[1] * s[1], v[2] * s[2], v[3] * s[3]);
-  uint32_t w1 = cvt4<FMT>(v[4] * s[4], v[5] * s[5], v[6] * s[6], v[7] * s[7]);
-  if (amax_bits > 0x7F800000u) {
-    w0 = patch_nan4(w0, &v[0]);
-    w1 = patch_nan4(w1, &v[4]);
+// Sum (or max) over the wave's four 16-lane rows of each of 8 values, spread out: lane 16 k + c gets those of its column
+// group c for the elements 2k and 2k + 1.  Each swap exchanges half of one register with half of another, so that
+// one addition serves two elements: 6 swaps and 6 additions for 8 values.
+template <class F>
+__device__ __forceinline__ void act_rows4(const float (&v)[8], float (&o)[2], F&& f) {
+  float r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[k]), __float_as_uint(v[k + 4]), false, false);
+    r[k] = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
   }
-  return u32x2{w0, w1};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[k]), __float_as_uint(r[k + 2]), false, false);
+    o[k] = f(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  }
+}
+
+// 8 values under 8 scales.  CLAMP: saturating; without, for scales that map the largest of the values to fmax (one
+// rounding of the product past it still converts to fmax)
+template <int FMT, bool CLAMP>
+__device__ __forceinline__ u32x2 act_cast8(const float (&v)[8], const float (&s)[8], uint32_t amax_bits) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = v[i] * s[i];
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* y = x + 4 * h;
+    if (CLAMP || amax_bits >= 0x7F800000u) {
+      w[h] = cvt4<FMT>(y[0], y[1], y[2], y[3]);
+    } else if constexpr (FMT == FP8_E4M3) {
+      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+      w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    } else {
+      const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], 0, false);
+      w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], lo, true);
+    }
+  }
+  if (amax_bits > 0x7F800000u) {
+    w[0] = patch_nan4(w[0], &v[0]);
+    w[1] = patch_nan4(w[1], &v[4]);
+  }
+  return u32x2{w[0], w[1]};
 }
 
 template <int OP, int FMT, bool BF16, bool TILE, bool EDGE>
@@ -157,8 +194,9 @@ __global__ void __launch_bounds__(512) act_ct_kernel(const void* __restrict__ dh
   static_assert(!(TILE && EDGE), "1x128 runs need whole tiles");
   __shared__ uint32_t lds[kActTile * kActPitch];
   __shared__ float csum[8][kActTile];
-  __shared__ uint32_t cred[8][kActTile];
+  __shared__ float cred[8][kActTile];
   __shared__ float cscale[kActTile];
+  __shared__ uint32_t not_finite;
   const int64_t nkb = (cols + kActTile - 1) / kActTile, nrb = (rows + kActTile - 1) / kActTile, ntiles = nkb * nrb;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int r16 = t >> 4, cg = t & 15;
@@ -190,9 +228,10 @@ __global__ void __launch_bounds__(512) act_ct_kernel(const void* __restrict__ dh
     for (int e = 0; e < 8; ++e) s8[e] = s;
   }
   uint32_t amax_acc = 0;
-  load_tile(blockIdx.x);
+  if constexpr (!TILE) load_tile(blockIdx.x);
   for (int64_t ix = blockIdx.x; ix < ntiles; ix += gridDim.x) {
     if (ix != (int64_t)blockIdx.x) __syncthreads();  // the previous tile's transpose is done with the LDS
+    if constexpr (TILE) load_tile(ix);
     int64_t rb, kb;
     tile_rc(ix, rb, kb);
     const int64_t r0 = rb * kActTile, c0 = kb * kActTile;
@@ -220,49 +259,43 @@ __global__ void __launch_bounds__(512) act_ct_kernel(const void* __restrict__ dh
         amax_acc = amax_acc > m ? amax_acc : m;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += v[e];
-        const u32x2 w = act_cast8<FMT>(v, s8, m);
+        const u32x2 w = act_cast8<FMT, true>(v, s8, m);
         store_q(p, w);
         lds[(r16 + 32 * p) * kActPitch + cg * 2] = w.x;
         lds[(r16 + 32 * p) * kActPitch + cg * 2 + 1] = w.y;
       }
       if (ix + gridDim.x < ntiles) load_tile(ix + gridDim.x);
     } else {
-      float v[4][8], srow[4];
-      uint32_t m[4];
+      float v[4][8], srow[4], cm[8], co[2];
+      if (t == 0) not_finite = 0u;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         in[p].results(v[p]);
-        m[p] = act_amax8(v[p]);
         float si;
-        current_scale<FMT>(group_max_u32<16>(m[p]), srow[p], si);
+        current_scale<FMT>(group_max_u32<16>(act_amax8(v[p])), srow[p], si);
         if (cg == 0) q_sinv[kb * rows + r0 + r16 + 32 * p] = si;  // [cols/128][rows]
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += v[p][e];
       }
-      if (ix + gridDim.x < ntiles) load_tile(ix + gridDim.x);
       // column runs: this thread's 4 rows, the wave's 4 lane groups, then the 8 waves
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) c = c > abs_bits(v[p][e]) ? c : abs_bits(v[p][e]);
-        uint32_t o = (uint32_t)__shfl_xor((int)c, 16, 64);
-        c = c > o ? c : o;
-        o = (uint32_t)__shfl_xor((int)c, 32, 64);
-        c = c > o ? c : o;
-        if (lane < 16) cred[wave][cg * 8 + e] = c;
-      }
+      for (int e = 0; e < 8; ++e) cm[e] = act_max3(act_max3(v[0][e], v[1][e], v[2][e]), v[3][e], v[3][e]);
+      act_rows4(cm, co, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
+      *reinterpret_cast<float2*>(&cred[wave][cg * 8 + 2 * (lane >> 4)]) = make_float2(co[0], co[1]);
       __syncthreads();
       if (t < kActTile) {
-        uint32_t c = cred[0][t];
+        uint32_t c = __float_as_uint(cred[0][t]);
 #pragma unroll
-        for (int w = 1; w < 8; ++w) c = c > cred[w][t] ? c : cred[w][t];
+        for (int w = 1; w < 8; ++w) c = c > __float_as_uint(cred[w][t]) ? c : __float_as_uint(cred[w][t]);
         float sc, si;
         current_scale<FMT>(c, sc, si);
         cscale[t] = sc;
+        if (c >= 0x7F800000u) not_finite = 0x7F800001u;
         qT_sinv[rb * cols + c0 + t] = si;  // [rows/128][cols]
       }
       __syncthreads();
+      // an infinity or NaN somewhere in the tile: its runs have scale 1, and the casts clamp and rewrite NaN
+      const uint32_t bad = not_finite;
       float scol[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) scol[e] = cscale[cg * 8 + e];
@@ -271,22 +304,16 @@ __global__ void __launch_bounds__(512) act_ct_kernel(const void* __restrict__ dh
         float sr[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sr[e] = srow[p];
-        store_q(p, act_cast8<FMT>(v[p], sr, m[p]));
-        const u32x2 w = act_cast8<FMT>(v[p], scol, m[p]);
+        store_q(p, act_cast8<FMT, false>(v[p], sr, bad));
+        const u32x2 w = act_cast8<FMT, false>(v[p], scol, bad);
         lds[(r16 + 32 * p) * kActPitch + cg * 2] = w.x;
         lds[(r16 + 32 * p) * kActPitch + cg * 2 + 1] = w.y;
       }
     }
     if (part != nullptr) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[e] += __shfl_xor(sum[e], 16, 64);
-        sum[e] += __shfl_xor(sum[e], 32, 64);
-      }
-      if (lane < 16) {
-        *reinterpret_cast<float4*>(&csum[wave][cg * 8]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-        *reinterpret_cast<float4*>(&csum[wave][cg * 8 + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
-      }
+      float so[2];
+      act_rows4(sum, so, [](float a, float b) { return a + b; });
+      *reinterpret_cast<float2*>(&csum[wave][cg * 8 + 2 * (lane >> 4)]) = make_float2(so[0], so[1]);
     }
     __syncthreads();
     if (part != nullptr && t < kActTile && (!EDGE || c0 + t < cols)) {
@@ -333,12 +360,12 @@ __global__ void __launch_bounds__(512) act_ct_kernel(const void* __restrict__ dh
     if (amax_slot != nullptr) {
       const uint32_t mx = wave_max_u32(amax_acc);
       __syncthreads();
-      if (lane == 0) cred[wave][0] = mx;
+      if (lane == 0) cred[wave][0] = __uint_as_float(mx);
       __syncthreads();
       if (t == 0) {
-        uint32_t bm = cred[0][0];
+        uint32_t bm = __float_as_uint(cred[0][0]);
 #pragma unroll
-        for (int w = 1; w < 8; ++w) bm = bm > cred[w][0] ? bm : cred[w][0];
+        for (int w = 1; w < 8; ++w) bm = bm > __float_as_uint(cred[w][0]) ? bm : __float_as_uint(cred[w][0]);
         if (bm > __hip_atomic_load(amax_slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(amax_slot, bm);
       }
     }
@@ -361,8 +388,8 @@ struct ActArgs {
 template <int OP, int FMT, bool BF16>
 static void launch_act(const ActArgs& a, bool tile) {
   const int64_t tiles = ((a.rows + kActTile - 1) / kActTile) * ((a.cols + kActTile - 1) / kActTile);
-  const int64_t cap = 3ll * device_cus();
-  const dim3 grid((unsigned)std::min(tiles, cap));
+  const int64_t cap = 24ll * device_cus();
+  const dim3 grid((unsigned)(tile ? tiles : std::min(tiles, cap)));
   uint32_t* slot = reinterpret_cast<uint32_t*>(a.amax);
 #define SFP8_ACT(TILE, EDGE)                                                                                          \
   hipLaunchKernelGGL((act_ct_kernel<OP, FMT, BF16, TILE, EDGE>), grid, dim3(512), 0, a.st, a.dh, a.pre, a.rows, a.cols, \
