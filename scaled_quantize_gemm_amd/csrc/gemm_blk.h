@@ -335,6 +335,15 @@ __global__ void __launch_bounds__(512, 1) gemm_blk_kernel(const uint8_t* __restr
   epi.template bias<Shape::NT>(gn, N, b);
   epi.with_act([&](auto act_c) {
     constexpr int ACT = decltype(act_c)::value;
+    // residual: all of the lane's runs before the first store
+    typename Epilogue<OUT, EPI>::template Run<ACT, NT> res[EPI == EPI_RESIDUAL ? 4 * TI : 1];
+    if constexpr (EPI == EPI_RESIDUAL) {
+#pragma unroll
+      for (int k = 0; k < 4 * TI; ++k) {
+        const int gm = m0 + slab_a + TI * (4 * g + k / TI) + k % TI;
+        if (gm < M && gn < N) epi.template fetch<ACT, NT>(res[k], gm, gn, N, quad);
+      }
+    }
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(512, 1) gemm_blk_kernel(const uint8_t* __restr
         }
         epi.pre(v, b);
         epi.aux(v, gm, gn, N, quad);
-        epi.template out<ACT>(v, gm, gn, N, quad);
+        epi.template out<ACT>(v, gm, gn, N, quad, res[EPI == EPI_RESIDUAL ? TI * jj + i : 0]);
       }
   });
   epi.finish(lane, reinterpret_cast<uint32_t*>(smem));

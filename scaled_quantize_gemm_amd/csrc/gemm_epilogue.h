@@ -24,7 +24,7 @@
 // compile-time constant (a runtime test inside the unrolled loop let the compiler evaluate
 // the GELU of every element whatever the activation, and select), and call, per lane, for
 // runs of W adjacent columns gn .. gn+W-1 (gn % W == 0) of one row gm:  pre() (bias), aux(),
-// out<ACT>();  and finish() once at the end (amax reduction).  `full` means all W columns
+// fetch() (the residual's run, ahead of a batch), out<ACT>();  and finish() once at the end (amax reduction).  `full` means all W columns
 // exist and a W-wide vector store is aligned (N % W == 0).
 #pragma once
 
@@ -136,25 +136,83 @@ struct Epilogue {
     }
   }
 
-  // activation and the output store
+  // The residual's run beside W result columns (W / 2 outputs for SwiGLU), packed as loaded; nothing in the other
+  // kinds.  A kernel fetches a batch of runs before it stores any of them: C may be the residual, so the
+  // compiler keeps every load behind the stores before it, and one load per store would wait out each latency.
   template <int ACT, int W>
-  __device__ __forceinline__ void out(float (&v)[W], int gm, int gn, int N, bool full) {
+  struct Run {
+    static constexpr int kOut = ACT == FP8_ACT_SWIGLU ? W / 2 : W;
+    static constexpr int kWords = EPI != EPI_RESIDUAL ? 1 : OUT == EPI_BF16 ? (kOut + 1) / 2 : kOut;
+    uint32_t w[kWords];
+  };
+  template <int ACT, int W>
+  __device__ __forceinline__ void fetch(Run<ACT, W>& r, int gm, int gn, int N, bool full) const {
+    if constexpr (EPI == EPI_RESIDUAL) {
+      constexpr int n = Run<ACT, W>::kOut, div = ACT == FP8_ACT_SWIGLU ? 2 : 1;
+      const size_t at = (size_t)gm * (N / div) + gn / div;
+      const int avail = (N - gn) / div;
+      if constexpr (OUT == EPI_BF16) {
+        const uint16_t* c = static_cast<const uint16_t*>(p.residual) + at;
+        if (full && n == 4) {
+          const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(c));
+          r.w[0] = x.x;
+          r.w[n > 2 ? 1 : 0] = n > 2 ? x.y : x.x;
+        } else if (full && n == 2) {
+          r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(c));
+        } else {
+#pragma unroll
+          for (int i = 0; i < n; i += 2) {
+            const uint32_t lo = full || i < avail ? c[i] : 0u;
+            const uint32_t hi = i + 1 < n && (full || i + 1 < avail) ? c[i + 1] : 0u;
+            r.w[i / 2] = lo | hi << 16;
+          }
+        }
+      } else {
+        const uint32_t* c = static_cast<const uint32_t*>(p.residual) + at;
+        if (full && n == 4) {
+          const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(c));
+#pragma unroll
+          for (int i = 0; i < n; ++i) r.w[i] = x[i];
+        } else if (full && n == 2) {
+          const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(c));
+#pragma unroll
+          for (int i = 0; i < n; ++i) r.w[i] = x[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < n; ++i) r.w[i] = full || i < avail ? c[i] : 0u;
+        }
+      }
+    }
+  }
+
+  // activation and the residual: W result columns -> o
+  template <int ACT, int W>
+  __device__ __forceinline__ void result(const float (&v)[W], float (&o)[Run<ACT, W>::kOut], const Run<ACT, W>& res) const {
     if constexpr (ACT == FP8_ACT_SWIGLU) {
       static_assert(W % 2 == 0, "SwiGLU needs column pairs");
-      float o[W / 2];
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) o[i] = swiglu(v[2 * i], v[2 * i + 1]);
-      add_residual<W / 2>(o, (size_t)gm * (N / 2) + gn / 2, full, (N - gn) / 2);
-      // output column gn/2 + i exists iff its up column gn + 2i + 1 does
-      emit<W / 2>(o, (size_t)gm * (N / 2) + gn / 2, full, (N - gn) / 2);
     } else {
-      if constexpr (ACT == FP8_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = gelu_exact(v[i]);
-      }
-      add_residual<W>(v, (size_t)gm * N + gn, full, N - gn);
-      emit<W>(v, (size_t)gm * N + gn, full, N - gn);
+      for (int i = 0; i < W; ++i) o[i] = ACT == FP8_ACT_GELU ? gelu_exact(v[i]) : v[i];
     }
+    if constexpr (EPI == EPI_RESIDUAL) {
+#pragma unroll
+      for (int i = 0; i < Run<ACT, W>::kOut; ++i) {
+        if constexpr (OUT == EPI_BF16) o[i] += (i & 1) ? bf16_hi(res.w[i / 2]) : bf16_lo(res.w[i / 2]);
+        else o[i] += __uint_as_float(res.w[i]);
+      }
+    }
+  }
+
+  // ... and the output store
+  template <int ACT, int W>
+  __device__ __forceinline__ void out(float (&v)[W], int gm, int gn, int N, bool full, const Run<ACT, W>& res) {
+    // SwiGLU: output column gn/2 + i exists iff its up column gn + 2i + 1 does
+    constexpr int div = ACT == FP8_ACT_SWIGLU ? 2 : 1;
+    float o[W / div];
+    result<ACT>(v, o, res);
+    emit<W / div>(o, (size_t)gm * (N / div) + gn / div, full, (N - gn) / div);
   }
 
   // every thread of the block, after its stores: fold the block's amax into the slot with one
@@ -179,19 +237,6 @@ struct Epilogue {
   }
 
  private:
-  // + the residual at element offset `at` (C's own layout and type); each element is read by the lane that
-  // then writes it, so C may be the residual
-  template <int W>
-  __device__ __forceinline__ void add_residual(float (&v)[W], size_t at, bool full, int avail) const {
-    if constexpr (EPI == EPI_RESIDUAL) {
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (full || i < avail)
-          v[i] += OUT == EPI_BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p.residual)[at + i] << 16)
-                                  : static_cast<const float*>(p.residual)[at + i];
-    }
-  }
-
   // W values to element offset `at` of the output; `avail` = how many of them exist
   template <int W>
   __device__ __forceinline__ void emit(const float (&v)[W], size_t at, bool full, int avail) {

@@ -15,6 +15,7 @@
 
 #include "gemm_blk.h"
 #include "gemm_small.h"
+#include "gemm_tokens.h"
 #include "gemm_w4.h"
 
 namespace sfp8 {
@@ -32,6 +33,9 @@ constexpr int64_t kSmallTileMax = 256;
 template <int MODE, int FA, int FB, int OUT, int EPI>
 static int launch_gemm(const uint8_t* A, const uint8_t* B, const void* sa, const void* sb, const EpiParams& ep, int M,
                        int N, int K, hipStream_t st, const char* what) {
+  if constexpr (EPI == EPI_RESIDUAL) {
+    if (tokens_apply<MODE>(M, N)) return launch_tokens<MODE, FA, OUT>(A, B, sa, sb, ep, M, N, K, st, what);
+  }
   if constexpr (MODE == MODE_TENSOR) {
     // fewer 256 x 256 tiles than CUs: the 256 x 128 tiles of the blockwise kernel keep twice
     // as many CUs busy (workload 2's per-tensor GEMMs 1.5x faster); from one full wave of

@@ -201,10 +201,21 @@ __global__ void __launch_bounds__(256) gemm_kernel(const uint8_t* __restrict__ A
       const int gn = n0 + wn * Cfg::WN + 16 * j + r;
       float b[1];
       epi.template bias<1>(gn, N, b);
+      // the residual of this column's rows (for SwiGLU the gate columns' lanes) before the first store
+      constexpr int W = ACT == FP8_ACT_SWIGLU ? 2 : 1;
+      typename Epilogue<OUT, EPI>::template Run<ACT, W> res[EPI == EPI_RESIDUAL ? 4 * Cfg::TM : 1];
+      if constexpr (EPI == EPI_RESIDUAL) {
+#pragma unroll
+        for (int k = 0; k < 4 * Cfg::TM; ++k) {
+          const int gm = m0 + wm * Cfg::WM + 16 * (k >> 2) + 4 * g + (k & 3);
+          if (gm < M && gn < N && (W == 1 || (r & 1) == 0)) epi.template fetch<ACT, W>(res[k], gm, gn, N, true);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < Cfg::TM; ++i)
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
+          const auto& rr = res[EPI == EPI_RESIDUAL ? 4 * i + jj : 0];
           const int gm = m0 + wm * Cfg::WM + 16 * i + 4 * g + jj;
           const bool in = gm < M && gn < N;
           float v[1] = {MODE == MODE_TENSOR ? acc[i][j][jj] * s : acc[i][j][jj]};
@@ -213,9 +224,9 @@ __global__ void __launch_bounds__(256) gemm_kernel(const uint8_t* __restrict__ A
           if constexpr (ACT == FP8_ACT_SWIGLU) {
             // the up value of an even (gate) column is held by the next lane
             float w[2] = {v[0], __shfl_xor(v[0], 1, 64)};
-            if (in && (r & 1) == 0) epi.template out<ACT>(w, gm, gn, N, true);
+            if (in && (r & 1) == 0) epi.template out<ACT>(w, gm, gn, N, true, rr);
           } else if (in) {
-            epi.template out<ACT>(v, gm, gn, N, true);
+            epi.template out<ACT>(v, gm, gn, N, true, rr);
           }
         }
     }
