@@ -466,7 +466,8 @@ extern "C" int fp8_act_cast_transpose(const void* pre, int dtype, int64_t rows, 
 
 extern "C" size_t fp8_act_backward_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows >= (1ll << 31) || cols >= (1ll << 31)) return 0;
-  return (size_t)((rows + kActTile - 1) / kActTile) * (size_t)cols * sizeof(float);
+  const int64_t tile_rows = (rows + kActTile - 1) / kActTile;
+  return tile_rows <= 1 ? 0 : (size_t)tile_rows * (size_t)cols * sizeof(float);
 }
 
 extern "C" int fp8_act_backward(const void* dh, const void* pre, int dtype, int64_t rows, int64_t cols, int act, int fmt,
@@ -483,14 +484,16 @@ extern "C" int fp8_act_backward(const void* dh, const void* pre, int dtype, int6
   SFP8_REQUIRE(dbias == nullptr || aligned4(dbias), FP8_ERR_ARG, "%s: misaligned dbias", what);
   if (cols == 0) return FP8_OK;
   hipStream_t st = (hipStream_t)stream;
-  float* part = dbias != nullptr ? static_cast<float*>(workspace) : nullptr;
+  // one tile row: its partial row is the sum itself
+  const int tile_rows = (int)((rows + kActTile - 1) / kActTile);
+  float* part = dbias == nullptr || tile_rows == 1 ? dbias : static_cast<float*>(workspace);
   if (rows > 0) {
     SFP8_REQUIRE(dh != nullptr && q != nullptr && qT != nullptr && (act == FP8_ACT_NONE || pre != nullptr), FP8_ERR_ARG,
                  "%s: null dh, pre, q or qT", what);
     SFP8_REQUIRE(aligned16(dh) && aligned16(pre) && aligned16(q) && aligned16(qT), FP8_ERR_ARG,
                  "%s: dh, pre, q, qT must be 16-byte aligned", what);
     const size_t need = fp8_act_backward_workspace(rows, cols);
-    SFP8_REQUIRE(dbias == nullptr || (workspace != nullptr && aligned16(workspace) && workspace_bytes >= need),
+    SFP8_REQUIRE(dbias == nullptr || need == 0 || (workspace != nullptr && aligned16(workspace) && workspace_bytes >= need),
                  FP8_ERR_ARG, "%s: dbias needs a workspace of %zu bytes, 16-byte aligned (%zu given)", what, need,
                  workspace_bytes);
     const ActArgs a = {dh, pre, rows, cols, scale, amax_slot, q, q_scale_inv, qT, qT_scale_inv, part, st};
@@ -501,7 +504,7 @@ extern "C" int fp8_act_backward(const void* dh, const void* pre, int dtype, int6
     const int rc2 = check_launch(what);
     if (rc2 != FP8_OK) return rc2;
   }
-  if (dbias == nullptr) return FP8_OK;
-  launch_col_reduce(part, (int)((rows + kActTile - 1) / kActTile), 1, cols, cols, dbias, nullptr, st);
+  if (dbias == nullptr || tile_rows == 1) return FP8_OK;
+  launch_col_reduce(part, tile_rows, 1, cols, cols, dbias, nullptr, st);
   return check_launch(what);
 }

@@ -13,30 +13,34 @@
 namespace sfp8 {
 
 struct GeluParts {
-  float cdf;   // Phi(x)
+  float tail;  // Phi(-|x|)
   float expo;  // e^(-x^2 / 2)
 };
 
 __device__ __forceinline__ GeluParts gelu_parts(float x) {
-  constexpr float q[9] = {0.1691880060075352f,   0.17071521302100234f, 0.1483392729403964f,
-                          0.21492564526538546f,  -0.09464973146101112f, 0.547718557973177f,
-                          -0.5122767787999469f, 0.48556256570665635f,  -0.12952277023763256f};
-  const float z = fabsf(x) * 0.70710678118654752440f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, z, 1.0f));
+  // halved: the tail is erfc / 2
+  constexpr float q[9] = {0.5f * 0.1691880060075352f,   0.5f * 0.17071521302100234f, 0.5f * 0.1483392729403964f,
+                          0.5f * 0.21492564526538546f,  0.5f * -0.09464973146101112f, 0.5f * 0.547718557973177f,
+                          0.5f * -0.5122767787999469f, 0.5f * 0.48556256570665635f,  0.5f * -0.12952277023763256f};
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f * 0.70710678118654752440f, fabsf(x), 1.0f));
   float p = q[8];
 #pragma unroll
   for (int i = 7; i >= 0; --i) p = fmaf(p, t, q[i]);
   const float e = __builtin_amdgcn_exp2f(x * x * -0.72134752044448170368f);
-  const float tail = 0.5f * t * p * e;
-  return {x < 0.0f ? tail : 1.0f - tail, e};
+  return {t * p * e, e};
 }
 
-__device__ __forceinline__ float act_gelu(float x) { return x * gelu_parts(x).cdf; }
+// x Phi(x) = max(x, 0) - |x| Phi(-|x|) for either sign (|x| held finite: an infinity times the tail's 0 is no number)
+__device__ __forceinline__ float act_gelu(float x) {
+  const float a = fminf(fabsf(x), 3.40282346638528859812e+38f);
+  const float h = fmaf(-a, gelu_parts(x).tail, fmaxf(x, 0.0f));
+  return h;
+}
 
 // d gelu / dx = Phi(x) + x phi(x)
 __device__ __forceinline__ float act_gelu_grad(float x) {
   const GeluParts g = gelu_parts(x);
-  return fmaf(x * 0.39894228040143267794f, g.expo, g.cdf);
+  return fmaf(x * 0.39894228040143267794f, g.expo, x < 0.0f ? g.tail : 1.0f - g.tail);
 }
 
 // s = sigmoid(g) and c = 1 - s = sigmoid(-g), both to fp32 accuracy at either sign of g: from

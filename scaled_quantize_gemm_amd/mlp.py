@@ -216,7 +216,7 @@ def fp8_act_backward(dh: torch.Tensor, pre: Optional[torch.Tensor], act: int, fm
     if with_bias:
         if dbias is None:
             dbias = torch.empty(cols, dtype=_F32, device=dh.device)
-        if workspace is None:
+        if workspace is None and need:
             workspace = torch.empty(need, dtype=_U8, device=dh.device)
     _launch(dh, lib.fp8_act_backward, dh.data_ptr(), p_pre, _hp_dtype(dh), rows, cols, act, fmt, granularity, p_scale,
             p_slot, q.data_ptr(), _ptr(q_scale_inv), qT.data_ptr(), _ptr(qT_scale_inv), _ptr(dbias), _ptr(workspace),

@@ -275,6 +275,20 @@ def test_zero_runs(sq):
     assert not (out[0] & 0x7F).any() and (out[1] == 1).all() and (out[3] == 1).all() and not out[4].any()
 
 
+def test_infinite_pre_activations(sq):
+    """GELU's limits at the infinities: +inf saturates and is the amax, -inf gives zero; nothing turns into NaN."""
+    pre = torch.ones((128, 256))
+    pre[3, 7], pre[4, 8] = float("inf"), -float("inf")
+    for dtype in (BF, F32):
+        slot = torch.zeros(1, device=DEV)
+        q, _, qT, _ = sq.fp8_act_cast_transpose(pre.to(dtype).to(DEV), GELU, 0, scale=torch.ones(1, device=DEV), amax_slot=slot)
+        assert q[3, 7] == 0x7E and q[4, 8] & 0x7F == 0 and torch.equal(qT, q.t()) and torch.isinf(slot).all()
+        q, qs, qT, qTs = sq.fp8_act_cast_transpose(pre.to(dtype).to(DEV), GELU, 0, granularity=1)
+        assert q[3, 7] == 0x7E and qT[7, 3] == 0x7E and qs[0, 3] == 1 and qTs[0, 7] == 1 and qs[0, 4] != 1
+        # a finite value under scale 1 beside the infinity: gelu(1) = 0.841 -> 0.8125 = 0x35
+        assert q[3, 8] == 0x35 and qT[7, 4] == 0x35
+
+
 def test_empty(sq):
     one = torch.ones(1, device=DEV)
     none = torch.empty((0, 256), dtype=BF, device=DEV)

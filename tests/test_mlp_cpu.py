@@ -79,10 +79,11 @@ def test_layernorm_backward_refusals(sq):
 
 @pytest.mark.parametrize("backward", [False, True])
 def test_act_refusals(sq, backward):
-    need = sq.fp8_act_backward_workspace(128, 256)
+    need = sq.fp8_act_backward_workspace(256, 256)
+    assert need > 0
     P = ctypes.c_void_p(0x200000)
 
-    def act(dh=FAKE, pre=FAKE, dt=1, r=128, c=256, a=1, fmt=0, gran=0, s=FAKE, slot=None, q=FAKE, qs=None, qT=FAKE,
+    def act(dh=FAKE, pre=FAKE, dt=1, r=256, c=256, a=1, fmt=0, gran=0, s=FAKE, slot=None, q=FAKE, qs=None, qT=FAKE,
             qTs=None, db=FAKE, ws=P, n=need):
         if backward:
             return sq.lib.fp8_act_backward(dh, pre, dt, r, c, a, fmt, gran, s, slot, q, qs, qT, qTs, db, ws, n, None)
@@ -162,10 +163,11 @@ def test_binding_rejects_mis_sized_buffers(sq):
     _raises(lambda: ac(granularity=1, scale=None, qT_scale_inv=e(1, 256)), ValueError, "qT_scale_inv must have")
     _raises(lambda: ac(scale=e(0)), ValueError, "at least 1")
     _raises(lambda: ac(), ValueError, "GPU tensor")
+    pre = e(256, 256, dtype=bf)
     ab = lambda **k: sq.fp8_act_backward(  # noqa: E731
-        **{**dict(dh=e(128, 128, dtype=bf), pre=pre, act=2, fmt=1, scale=one), **k})
+        **{**dict(dh=e(256, 128, dtype=bf), pre=pre, act=2, fmt=1, scale=one), **k})
     _raises(lambda: ab(dh=pre), ValueError, "dh must have shape")
-    _raises(lambda: ab(dh=e(128, 128)), TypeError, "pre must be")
+    _raises(lambda: ab(dh=e(256, 128)), TypeError, "pre must be")
     _raises(lambda: ab(pre=None), ValueError, "pre is required")
     _raises(lambda: ab(dbias=e(128)), ValueError, "dbias must have")
     _raises(lambda: ab(qT=e(128, 256, dtype=u8)), ValueError, "qT must have")
