@@ -89,7 +89,8 @@ size_t fp8_layernorm_backward_workspace(int64_t rows, int64_t cols);
  *              scale per 1x128 run, q_scale_inv = fp32 [H/128][rows]; qT with one per 128x1 run of
  *              h, qT_scale_inv = fp32 [rows/128][H].  rows % 128 == 0, H % 128 == 0; scale and
  *              amax_slot must be NULL.
- *   q, qT      device uint8.  Empty inputs are a no-op.
+ *   q, qT      device uint8.  Empty inputs are a no-op.  GELU of +inf is +inf, of -inf 0; elements
+ *   that are not finite are cast as fp8_quantize casts them.
  *   Alignment: pre, q, qT 16-byte; fp32 scalars and arrays 4-byte.
  *   Errors: FP8_ERR_ARG, FP8_ERR_SHAPE, FP8_ERR_DTYPE.
  */
@@ -106,6 +107,8 @@ int fp8_act_cast_transpose(const void *pre, int dtype, int64_t rows, int64_t col
  *              FP8_ACT_GELU:   d = dh * (Phi(v) + v * phi(v)), phi the normal density
  *              FP8_ACT_SWIGLU: with s = 1 / (1 + e^-g): d[2f] = dh[f] * u * s * (1 + g (1 - s)),
  *                              d[2f+1] = dh[f] * g * s  (g = v[2f], u = v[2f+1])
+ *   A pre-activation that is not finite gives what fp32 arithmetic makes of these formulas (NaN for
+ *   an infinity times 0); its element alone is touched, in its tile's runs scale 1.
  *   q [rows][cols], qT [cols][rows], scale, amax_slot, q_scale_inv, qT_scale_inv: d cast as
  *   fp8_act_cast_transpose casts h (the shapes with cols in place of H).
  *   dbias      device fp32 [cols]: sum over the rows of d in fp32, before the cast; or NULL.
@@ -118,7 +121,7 @@ int fp8_act_backward(const void *dh, const void *pre, int dtype, int64_t rows, i
                      int granularity, const float *scale, float *amax_slot, uint8_t *q, float *q_scale_inv,
                      uint8_t *qT, float *qT_scale_inv, float *dbias, void *workspace, size_t workspace_bytes,
                      void *stream);
-/* Bytes of workspace for that call (0 for sizes it refuses). */
+/* Bytes of workspace for that call with dbias (0 where it needs none, and for sizes it refuses). */
 size_t fp8_act_backward_workspace(int64_t rows, int64_t cols);
 
 /*

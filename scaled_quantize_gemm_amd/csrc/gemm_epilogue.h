@@ -24,8 +24,9 @@
 // compile-time constant (a runtime test inside the unrolled loop let the compiler evaluate
 // the GELU of every element whatever the activation, and select), and call, per lane, for
 // runs of W adjacent columns gn .. gn+W-1 (gn % W == 0) of one row gm:  pre() (bias), aux(),
-// fetch() (the residual's run, ahead of a batch), out<ACT>();  and finish() once at the end (amax reduction).  `full` means all W columns
-// exist and a W-wide vector store is aligned (N % W == 0).
+// fetch() (the residual's run, a batch of runs ahead of the stores), out<ACT>();  and finish()
+// once at the end (amax reduction).  `full` means all W columns exist and a W-wide vector store
+// is aligned (N % W == 0).
 #pragma once
 
 #include <type_traits>

@@ -7,7 +7,7 @@
 // (accumulation-precision bullet); MX gives every 32 numbers a shared scale and DeepSeek-V3
 // scales 1x128 activation runs and 128x128 weight blocks (absmax bullet).
 //
-// Kernels: gemm_small.h (128 x 128 tiles, any shape), gemm_w4.h (256 x 256, one wave per SIMD,
+// Kernels: gemm_tokens.h (a few rows, residual epilogue), gemm_small.h (128 x 128 tiles, any shape), gemm_w4.h (256 x 256, one wave per SIMD,
 // per-tensor and MX), gemm_blk.h (256 x 128 / 256 x 64 ping-pong, blockwise and small per-tensor
 // problems).
 // This file routes a problem to one of them and holds the host-side checks and dispatch.

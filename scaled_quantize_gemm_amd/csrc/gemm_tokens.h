@@ -139,7 +139,8 @@ constexpr int kTokRows = 64, kTokRowsWide = 32, kTokWideN = 12288;
 
 template <int MODE>
 static bool tokens_apply(int M, int N) {
-  return M <= (MODE == MODE_TENSOR && N >= kTokWideN ? kTokRowsWide : kTokRows);
+  // (a launch holds less than 2^32 threads)
+  return M <= (MODE == MODE_TENSOR && N >= kTokWideN ? kTokRowsWide : kTokRows) && N <= (1 << 24);
 }
 
 // Tiles of 16 columns per block: as many as leave about a block per CU, so that A is read by fewer blocks (14336 x 4096

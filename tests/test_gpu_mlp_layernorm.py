@@ -229,3 +229,14 @@ def test_dbeta_may_be_left_out(sq):
                                        rs.data_ptr(), None, dx.data_ptr(), dg.data_ptr(), None, ws.data_ptr(), n, None)
     torch.cuda.synchronize()
     assert rc == sq.FP8_OK and torch.equal(dx, ref[0]) and torch.equal(dg, ref[1])
+
+
+def test_one_row_given_as_a_vector(sq):
+    rng = np.random.default_rng(11)
+    x, g, dy = _rand(rng, 300, dtype=BF).to(DEV), _rand(rng, 300, 0.1, 1.0).to(DEV), _rand(rng, 300, dtype=BF).to(DEV)
+    mu, rs = torch.empty(2, 1, device=DEV).unbind(0)
+    y = sq.fp8_layernorm(x, g, None, EPS, mu=mu, rsigma=rs)
+    assert y.shape == (300,) and torch.equal(y, sq.fp8_layernorm(x[None], g, None, EPS)[0])
+    dx, dg, db = sq.fp8_layernorm_backward(dy, x, g, mu, rs)
+    ref = sq.fp8_layernorm_backward(dy[None], x[None], g, mu, rs)
+    assert dx.shape == (300,) and torch.equal(dx, ref[0][0]) and torch.equal(dg, ref[1]) and torch.equal(db, ref[2])

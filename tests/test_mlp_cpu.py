@@ -184,6 +184,36 @@ def test_binding_rejects_mis_sized_buffers(sq):
     _raises(lambda: gr(e(8, 16)), ValueError, "GPU tensor")
 
 
+def test_a_launch_makes_the_tensors_device_current(sq, monkeypatch):
+    """Tensors on another device than the current one: the call runs with theirs current, on their stream."""
+    import contextlib
+
+    from scaled_quantize_gemm_amd import mlp
+
+    class Tensor:
+        device = "cuda:1"
+
+        def get_device(self):
+            return 1
+
+    seen = []
+
+    @contextlib.contextmanager
+    def device(d):
+        seen.append(("enter", d))
+        yield
+        seen.append(("exit", d))
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(mlp, "_stream", lambda t: 77)
+    for current in (1, 0):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+        mlp._launch(Tensor(), lambda *a: seen.append(a) or 0, 5)
+    assert seen == [(5, 77), ("enter", "cuda:1"), (5, 77), ("exit", "cuda:1")]
+    with pytest.raises(sq.Fp8Error):
+        mlp._launch(Tensor(), lambda *a: sq.FP8_ERR_ARG)
+
+
 # ------------------------------------------------------------------ the oracle's gradients against differences
 
 
