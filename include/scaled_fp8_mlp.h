@@ -72,7 +72,7 @@ int fp8_layernorm_backward(const void *dy, int dy_dtype, const void *x, int x_dt
                            const void *gamma, int w_dtype, const float *mu, const float *rsigma, const void *dres,
                            void *dx, float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes,
                            void *stream);
-/* Bytes of workspace for that call (0 for sizes it refuses). */
+/* Bytes of workspace for that call (0 where it needs none, and for sizes it refuses). */
 size_t fp8_layernorm_backward_workspace(int64_t rows, int64_t cols);
 
 /*

@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(LnBlock<W>::kThreads) ln_bwd_kernel(const void
                                                                       const float* __restrict__ mu,
                                                                       const float* __restrict__ rsig, const void* dres,
                                                                       int64_t rows, int cols, void* dx,
-                                                                      float* __restrict__ part) {
+                                                                      float* __restrict__ part,
+                                                                      float* __restrict__ dgamma,
+                                                                      float* __restrict__ dbeta) {
   constexpr int G = LnBlock<W>::kTeams;
   constexpr bool KEEP = NCH <= 2;
   constexpr int XB = XBF ? 2 : 4, DB = DBF ? 2 : 4;
@@ -377,7 +379,8 @@ __global__ void __launch_bounds__(LnBlock<W>::kThreads) ln_bwd_kernel(const void
       ln_store<XBF, TAIL>(out, col[p], cols, o);
     }
   }
-  // the teams' column sums, added one team after the other, the last one to the block's partial row [2][pitch]
+  // the teams' column sums, added one team after the other, the last one to the block's partial row [2][pitch], or
+  // (part null: the only block) to dgamma and dbeta
   const int pitch = ln_pitch(cols);
   float* mine = part + (int64_t)blockIdx.x * 2 * pitch;
 #pragma unroll 1
@@ -400,7 +403,15 @@ __global__ void __launch_bounds__(LnBlock<W>::kThreads) ln_bwd_kernel(const void
               }
               if (t < G - 1) *at = sum;
             }
-            if (t == G - 1) *reinterpret_cast<float4*>(mine + h * pitch + col[p] + i) = sum;
+            if (t < G - 1) continue;
+            if (part != nullptr) {
+              *reinterpret_cast<float4*>(mine + h * pitch + col[p] + i) = sum;
+            } else if (float* out = h == 0 ? dgamma : dbeta) {
+              const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (!TAIL || col[p] + i + k < cols) out[col[p] + i + k] = o[k];
+            }
           }
       }
     }
@@ -445,11 +456,14 @@ static void ln_types(bool a, bool b, bool c, F&& f) {
 }
 
 // blocks of the backward: at most 256, one per CU, each with a partial row of dgamma and dbeta (512 took 6 us more on
-// 8192 x 4096: twice the partial rows to write and join)
-constexpr int64_t kLnBwdBlocks = 256;
+// 8192 x 4096: twice the partial rows to write and join); up to 4 rows per team one block does it all, without the
+// partial row, the workspace and the second launch (16 x 768: a call 13.9 us, 6.7 in a graph; 17 x 768, with them: 18.2 and
+// 6.2)
+constexpr int64_t kLnBwdBlocks = 256, kLnAloneRows = 4;
 static int64_t ln_bwd_blocks(int64_t rows, int64_t cols) {
   int64_t teams = 1;
   ln_shape<true>(cols, [&](auto w, auto) { teams = LnBlock<decltype(w)::value>::kTeams; });
+  if (rows <= kLnAloneRows * teams) return rows > 0;
   return std::min(kLnBwdBlocks, (rows + teams - 1) / teams);
 }
 
@@ -495,7 +509,8 @@ extern "C" int fp8_layernorm(const void* x, int x_dtype, int64_t rows, int64_t c
 
 extern "C" size_t fp8_layernorm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || rows >= (1ll << 31) || cols < 0 || cols > kLnMaxCols) return 0;
-  return (size_t)ln_bwd_blocks(rows, cols) * 2 * (size_t)ln_pitch(cols) * sizeof(float);
+  const int64_t blocks = ln_bwd_blocks(rows, cols);
+  return blocks <= 1 ? 0 : (size_t)blocks * 2 * (size_t)ln_pitch(cols) * sizeof(float);
 }
 
 extern "C" int fp8_layernorm_backward(const void* dy, int dy_dtype, const void* x, int x_dtype, int64_t rows,
@@ -515,7 +530,7 @@ extern "C" int fp8_layernorm_backward(const void* dy, int dy_dtype, const void* 
   hipStream_t st = (hipStream_t)stream;
   const int wb = w_dtype == HP_BF16, c = (int)cols;
   const int64_t blocks = ln_bwd_blocks(rows, cols);
-  float* part = static_cast<float*>(workspace);
+  float* part = blocks == 1 ? nullptr : static_cast<float*>(workspace);
   if (rows > 0) {
     SFP8_REQUIRE(dy != nullptr && x != nullptr && gamma != nullptr && mu != nullptr && rsigma != nullptr && dx != nullptr,
                  FP8_ERR_ARG, "%s: null dy, x, gamma, mu, rsigma or dx", what);
@@ -525,19 +540,20 @@ extern "C" int fp8_layernorm_backward(const void* dy, int dy_dtype, const void* 
     SFP8_REQUIRE(dx != dy || dy_dtype == x_dtype, FP8_ERR_ARG, "%s: dx may be dy only where dy has x's type", what);
     SFP8_REQUIRE(dx != x, FP8_ERR_ARG, "%s: dx may not be x", what);
     const size_t need = fp8_layernorm_backward_workspace(rows, cols);
-    SFP8_REQUIRE(workspace != nullptr && aligned16(workspace) && workspace_bytes >= need, FP8_ERR_ARG,
+    SFP8_REQUIRE(need == 0 || (workspace != nullptr && aligned16(workspace) && workspace_bytes >= need), FP8_ERR_ARG,
                  "%s: workspace of %zu bytes, 16-byte aligned, needed (%zu given)", what, need, workspace_bytes);
     ln_shape<true>(cols, [&](auto wc, auto nc) {
       constexpr int W = decltype(wc)::value, NCH = decltype(nc)::value;
       ln_types(x_dtype == HP_BF16, dy_dtype == HP_BF16, cols % 8 != 0, [&](auto xb, auto db, auto tail) {
         hipLaunchKernelGGL((ln_bwd_kernel<W, NCH, decltype(xb)::value, decltype(db)::value, decltype(tail)::value>),
                            dim3((unsigned)blocks), dim3(LnBlock<W>::kThreads), 0, st, dy, x, gamma, wb, mu, rsigma,
-                           dres, rows, c, dx, part);
+                           dres, rows, c, dx, part, dgamma, dbeta);
       });
     });
     const int rc = check_launch(what);
     if (rc != FP8_OK) return rc;
   }
+  if (blocks == 1) return FP8_OK;
   launch_col_reduce(part, (int)blocks, 2, ln_pitch(cols), cols, dgamma, dbeta, st);
   return check_launch(what);
 }

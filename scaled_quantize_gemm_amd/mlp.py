@@ -128,11 +128,11 @@ def fp8_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tenso
         dgamma = torch.empty_like(gamma, dtype=_F32)
     if dbeta is None:
         dbeta = torch.empty_like(gamma, dtype=_F32)
-    if workspace is None:
+    if workspace is None and need:
         workspace = torch.empty(need, dtype=_U8, device=x.device)
     _launch(x, lib.fp8_layernorm_backward, p_dy, _hp_dtype(dy), x.data_ptr(), _hp_dtype(x), rows, cols, p_gamma,
             _hp_dtype(gamma), p_mu, p_rs, p_dres, dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
+            _ptr(workspace), workspace.numel() if workspace is not None else 0)
     return dx, dgamma, dbeta
 
 

@@ -111,8 +111,8 @@ def test_backward_shapes(sq, shape, xt, dt):
 
 
 # few rows and many: one block, fewer rows than blocks, several rows per wave, a ragged last round
-@pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 129, 300, 1023, 2051, 5000])
-@pytest.mark.parametrize("cols", [96, 771])
+@pytest.mark.parametrize("rows", [1, 2, 4, 5, 8, 9, 15, 16, 17, 32, 33, 63, 129, 300, 1023, 2051, 5000])
+@pytest.mark.parametrize("cols", [96, 771, 2304])
 def test_backward_row_counts(sq, rows, cols):
     check_backward(sq, np.random.default_rng(rows + cols), rows, cols, BF, BF, dres=rows % 2 == 0)
 
@@ -198,7 +198,11 @@ def test_constant_and_non_finite_rows(sq):
 def test_other_stream_and_caller_buffers(sq):
     """Buffers of the caller on a stream of its own; neighbours of the outputs stay as they were."""
     rng = np.random.default_rng(9)
-    R, C = 130, 771
+    for R, C in ((130, 771), (9, 771), (3, 4100)):
+        _check_room(sq, rng, R, C)
+
+
+def _check_room(sq, rng, R, C):
     x, g, dy = _rand(rng, (R, C)).to(DEV), _rand(rng, C, 0.1, 1.0).to(DEV), _rand(rng, (R, C)).to(DEV)
     mu, rs = x.mean(1), 1 / x.std(1)
     ref = sq.fp8_layernorm_backward(dy, x, g, mu, rs)

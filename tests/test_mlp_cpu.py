@@ -53,10 +53,10 @@ def test_layernorm_refusals(sq):
 
 def test_layernorm_backward_refusals(sq):
     f = sq.lib.fp8_layernorm_backward
-    need = sq.fp8_layernorm_backward_workspace(4, 768)
+    need = sq.fp8_layernorm_backward_workspace(40, 768)
     P, Q = ctypes.c_void_p(0x200000), ctypes.c_void_p(0x300000)
 
-    def lnb(dy=FAKE, dt=1, x=P, xt=1, r=4, c=768, g=FAKE, wt=1, mu=FAKE, rs=FAKE, dres=None, dx=Q, dg=FAKE, db=None,
+    def lnb(dy=FAKE, dt=1, x=P, xt=1, r=40, c=768, g=FAKE, wt=1, mu=FAKE, rs=FAKE, dres=None, dx=Q, dg=FAKE, db=None,
             ws=FAKE, n=need):
         return f(dy, dt, x, xt, r, c, g, wt, mu, rs, dres, dx, dg, db, ws, n, None)
 
@@ -74,6 +74,7 @@ def test_layernorm_backward_refusals(sq):
     assert lnb(dy=Q, dt=0) == sq.FP8_ERR_ARG  # dx = dy of another type
     assert lnb(dy=None, c=0) == sq.FP8_OK
     w = sq.fp8_layernorm_backward_workspace
+    assert w(4, 768) == 0  # one block
     assert w(-1, 768) == w(4, 32769) == w(1 << 31, 8) == w(4, -8) == 0
 
 
@@ -134,23 +135,23 @@ def _raises(fn, exc, match):
 def test_binding_rejects_mis_sized_buffers(sq):
     bf, u8 = torch.bfloat16, torch.uint8
     e = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype)  # noqa: E731
-    x, g = e(6, 40, dtype=bf), e(40)
+    x, g = e(60, 40, dtype=bf), e(40)
     ln = sq.fp8_layernorm
     _raises(lambda: ln(x.half(), g, None, 1e-5), TypeError, "x must be")
     _raises(lambda: ln(x, e(39), None, 1e-5), ValueError, "gamma must have")
     _raises(lambda: ln(x, g, e(40, dtype=bf), 1e-5), TypeError, "beta must be")
     _raises(lambda: ln(x, g, None, 1e-5, sq.OUT_E4M3), ValueError, "OUT_F32 or OUT_BF16")
-    _raises(lambda: ln(x, g, None, 1e-5, y=e(6, 40)), TypeError, "y must be")
+    _raises(lambda: ln(x, g, None, 1e-5, y=e(60, 40)), TypeError, "y must be")
     _raises(lambda: ln(x, g, None, 1e-5, mu=e(5)), ValueError, "mu must have")
-    _raises(lambda: ln(e(40, 6, dtype=bf).t(), g, None, 1e-5), ValueError, "contiguous")
+    _raises(lambda: ln(e(40, 60, dtype=bf).t(), g, None, 1e-5), ValueError, "contiguous")
     _raises(lambda: ln(e(2, 3, 40), g, None, 1e-5), ValueError, "1-D or 2-D")
     _raises(lambda: ln(x, g, None, 1e-5), ValueError, "GPU tensor")
-    lb = lambda **k: sq.fp8_layernorm_backward(**{**dict(dy=x, x=x, gamma=g, mu=e(6), rsigma=e(6)), **k})  # noqa: E731
-    _raises(lambda: lb(dy=e(6, 39)), ValueError, "dy must have")
-    _raises(lambda: lb(mu=e(6, 1)), ValueError, "mu must have")
-    _raises(lambda: lb(rsigma=e(6, dtype=bf)), TypeError, "rsigma must be")
-    _raises(lambda: lb(dres=e(6, 40)), TypeError, "dres must be")
-    _raises(lambda: lb(dx=e(6, 41, dtype=bf)), ValueError, "dx must have")
+    lb = lambda **k: sq.fp8_layernorm_backward(**{**dict(dy=x, x=x, gamma=g, mu=e(60), rsigma=e(60)), **k})  # noqa: E731
+    _raises(lambda: lb(dy=e(60, 39)), ValueError, "dy must have")
+    _raises(lambda: lb(mu=e(60, 1)), ValueError, "mu must have")
+    _raises(lambda: lb(rsigma=e(60, dtype=bf)), TypeError, "rsigma must be")
+    _raises(lambda: lb(dres=e(60, 40)), TypeError, "dres must be")
+    _raises(lambda: lb(dx=e(60, 41, dtype=bf)), ValueError, "dx must have")
     _raises(lambda: lb(dgamma=e(40, dtype=bf)), TypeError, "dgamma must be")
     _raises(lambda: lb(dbeta=e(41)), ValueError, "dbeta must have")
     _raises(lambda: lb(workspace=e(8, dtype=u8)), ValueError, "at least")
